@@ -403,6 +403,9 @@ typedef enum tp_dtype {
  * (rows fp32, for the gradient) may be NULL. sum and out may be x or residual
  * itself (same pointer, row stride and type); any other overlap with an
  * output is TP_ERR_OVERLAP. 0 <= rows <= 2^31, 0 <= cols <= 2^24, eps >= 0.
+ * A row with a NaN is NaN throughout. A row with an infinity, or whose sum of
+ * squares passes fp32 (numbers of about 1.8e19), has rstd 0: its finite numbers
+ * give 0, an infinity gives NaN. A row of zeros with eps 0 is NaN.
  */
 TP_API int tp_rms_norm(const void *x, int64_t x_stride, const void *residual,
                        int64_t residual_stride, const void *weight, int64_t rows, int64_t cols,
