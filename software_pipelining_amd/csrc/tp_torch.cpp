@@ -142,7 +142,7 @@ PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n)
         c10::Device d(c10::kCUDA);
         Matrix x, r{};
         if (n != 6 || !device_of(args[0], d) || !matrix(args[0], d, x) || x.rows == 0 || x.cols == 0 ||
-            !PyFloat_Check(args[2]) || !PyLong_Check(args[4]))
+            !PyFloat_Check(args[2]) || !PyLong_Check(args[4]) || !PyBool_Check(args[5]))
             Py_RETURN_NONE;
         const at::ScalarType type = x.t->scalar_type();
         const int code = number_code(type);
@@ -215,7 +215,7 @@ PyObject *block_quantize(PyObject *, PyObject *const *args, Py_ssize_t n)
         c10::Device d(c10::kCUDA);
         Matrix x;
         if (n != 5 || !device_of(args[0], d) || !matrix(args[0], d, x) || x.rows == 0 || x.cols == 0 ||
-            !PyLong_Check(args[1]))
+            !PyLong_Check(args[1]) || !PyBool_Check(args[2]) || !PyBool_Check(args[3]) || !PyBool_Check(args[4]))
             Py_RETURN_NONE;
         const int code = number_code(x.t->scalar_type());
         const int eight = (int)PyLong_AsLong(args[1]);

@@ -244,7 +244,7 @@ def block_quantize(x, out_format: str = "e4m3", square: bool = False, straight: 
         qt = _eight_bit_empty(cols, rows, eight, device)
         scale_t = _empty(across if square else cols, down, dtype=torch.float32, device=device)
     if rows and cols:
-        _call("tp_block_quantize", device, x.data_ptr(), xs, rows, cols, _DTYPES[x.dtype], int(square),
+        _call("tp_block_quantize", device, x.data_ptr(), xs, rows, cols, _DTYPES[x.dtype], int(bool(square)),
               _EIGHT[eight], _ptr(q), cols + 15 & ~15, _ptr(scale), _ptr(qt), rows + 15 & ~15,
               _ptr(scale_t))
     return BlockQuantized(q, scale, qt, scale_t)
