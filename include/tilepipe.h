@@ -490,8 +490,10 @@ TP_API int tp_plan_chunk_copy(const void *src, const void *dst, int64_t n_chunks
 TP_API int tp_plan_workgroup_copy(const void *src, const void *dst, int64_t n_chunks,
                                   const void *workspace, int64_t workspace_bytes,
                                   const int32_t *status, int spin_limit, tp_plan *plan);
-/* For the 8-bit layer's operators the plan's threads and grid are those of the
- * main kernel, num_tiles its rows or tiles. */
+/* For the 8-bit layer's operators the plan's threads, grid and lds_bytes (the
+ * quantiser's static LDS among them) are those of the main kernel, num_tiles its
+ * rows or tiles, and a product's stages the LDS slots that its operands' blocks
+ * pass through. */
 TP_API int tp_plan_rms_norm(const void *x, int64_t x_stride, const void *residual,
                             int64_t residual_stride, const void *weight, int64_t rows, int64_t cols,
                             int dtype, float eps, const void *sum, int64_t sum_stride,

@@ -246,6 +246,7 @@ struct Tile {
     // a chunk that a row's end cuts is put together here only where registers
     // allow it
     static constexpr bool cut_rows = tm * tn <= 64 * 64;
+    static_assert(lds_bytes == matmul_tile_lds(BM, BN, Stages), "the planner's");
     static_assert(BM + BN <= threads && BM % 64 == 0, "one row's scales a lane");
     static_assert(a_loads * waves * 1024 == a_bytes && b_loads * waves * 1024 == b_bytes, "whole loads");
     static_assert(a_loads % 2 == 0 && b_loads % 2 == 0, "a wave's loads start at an even one");
@@ -494,12 +495,13 @@ __global__ void __launch_bounds__(64 * GM * GN) block_matmul_kernel(MatmulParams
 // bytes a row: one block's at a time, a line a row, they took as long as a's
 // and b's numbers together. Bound by the bytes of b and the latency to the
 // first of them: 1 x 8192 x 4096 (34 MB) 7.9 us, 4.3 TB/s; 48 x 4096 x 8192 9.9.
-constexpr int kSkinnyWaves = 8;
 template <int MT, int Slots>
 struct Skinny {
     static constexpr int slot = (MT + 1) * 2048;         // a's rows, b's rows
     static constexpr int scales = (MT + 1) * 256;        // of four blocks
     static constexpr int wave_lds = Slots * slot + 2 * scales;
+    static constexpr int lds_bytes = kSkinnyWaves * wave_lds;
+    static_assert(lds_bytes == matmul_skinny_lds(16 * MT, Slots), "the planner's");
 };
 
 template <int FA, int FB, bool Wide, bool Square, int MT, int Slots>

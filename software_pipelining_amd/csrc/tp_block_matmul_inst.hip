@@ -14,21 +14,21 @@ int launch(Fn fn, dim3 grid, int threads, int lds, const MatmulParams &p, void *
                                 (size_t)lds, (hipStream_t)stream);
 }
 
-template <bool Wide, bool Square, int BM, int BN, int GM, int GN, int Stages>
-int launch_tile(const MatmulParams &p, void *stream)
+template <bool Wide, bool Square, int Shape, int BM, int BN, int GM, int GN>
+int launch_tile(const MatmulPlan &plan, const MatmulParams &p, void *stream)
 {
+    constexpr int Stages = matmul_stages(Shape);
     using S = dev::Tile<BM, BN, GM, GN, Stages, Wide ? 4 : 8>;
-    const int64_t groups = op_ceil((int64_t)p.tiles_m * p.tiles_n * p.splits, 8) * 8;
     return launch(&dev::block_matmul_kernel<TP_INST_FA, TP_INST_FB, Wide, Square, BM, BN, GM, GN, Stages>,
-                  dim3((uint32_t)groups), S::threads, S::lds_bytes, p, stream);
+                  dim3((uint32_t)plan.grid), S::threads, S::lds_bytes, p, stream);
 }
 
 template <bool Wide, bool Square, int MT, int Slots>
 int launch_skinny(const MatmulParams &p, void *stream)
 {
     return launch(&dev::block_matmul_skinny_kernel<TP_INST_FA, TP_INST_FB, Wide, Square, MT, Slots>,
-                  dim3((uint32_t)p.tiles_n, (uint32_t)p.splits), 64 * dev::kSkinnyWaves,
-                  dev::kSkinnyWaves * dev::Skinny<MT, Slots>::wave_lds, p, stream);
+                  dim3((uint32_t)p.tiles_n, (uint32_t)p.splits), 64 * kSkinnyWaves,
+                  dev::Skinny<MT, Slots>::lds_bytes, p, stream);
 }
 
 template <bool Wide, bool Square>
@@ -38,27 +38,23 @@ int launch_shape(const MatmulPlan &plan, const MatmulParams &p, void *stream)
     case kMatmulSkinny:
         switch (plan.tile_m) {
         case 16:
-            // blocks of a wave: with more than 4 a second slot pays (1 x 16384 x
-            // 8192: 28.3 us against 30.3), with fewer the smaller LDS does (1 x
-            // 8192 x 4096: 9.7 against 10.1); more rows of a fill one slot's time
-            return op_ceil(p.blocks, p.splits * dev::kSkinnyWaves) > 4 ? launch_skinny<Wide, Square, 1, 2>(p, stream)
-                                                                       : launch_skinny<Wide, Square, 1, 1>(p, stream);
+            return plan.stages == 2 ? launch_skinny<Wide, Square, 1, 2>(p, stream)
+                                    : launch_skinny<Wide, Square, 1, 1>(p, stream);
         case 32: return launch_skinny<Wide, Square, 2, 1>(p, stream);
         case 48: return launch_skinny<Wide, Square, 3, 1>(p, stream);
         default: return launch_skinny<Wide, Square, 4, 1>(p, stream);
         }
     case kMatmul64:
-        // (with a fourth stage 1 to 3 % slower)
-        return launch_tile<Wide, Square, 64, 64, 1, 2, 3>(p, stream);
+        return launch_tile<Wide, Square, kMatmul64, 64, 64, 1, 2>(plan, p, stream);
     case kMatmul128:
-        return launch_tile<Wide, Square, 128, 128, 2, 2, 2>(p, stream);
+        return launch_tile<Wide, Square, kMatmul128, 128, 128, 2, 2>(plan, p, stream);
     case kMatmul128x256:
-        return launch_tile<Wide, Square, 128, 256, 2, 4, 3>(p, stream);
+        return launch_tile<Wide, Square, kMatmul128x256, 128, 256, 2, 4>(plan, p, stream);
     default:
         if constexpr (Wide)
             return (int)hipErrorInvalidValue;    // matmul_plan has no such plan
         else
-            return launch_tile<Wide, Square, 256, 256, 4, 2, 2>(p, stream);
+            return launch_tile<Wide, Square, kMatmul256, 256, 256, 4, 2>(plan, p, stream);
     }
 }
 

@@ -30,6 +30,7 @@ struct QuantLds {
     float2 col_scale[kOpBlock];
     alignas(16) uint8_t turned[kOpBlock * kOpBlock];
 };
+static_assert(sizeof(QuantLds) == kQuantLdsBytes, "the planner's");
 
 // The elements of a row of fewer than eight.
 template <class T>

@@ -60,12 +60,12 @@ bool is_number_type(int type) { return type == TP_BF16 || type == TP_FP16 || typ
 bool is_eight_bit(int type) { return type == TP_E4M3 || type == TP_E5M2; }
 bool aligned(uintptr_t p, int bytes) { return p % (uintptr_t)bytes == 0; }
 
-void fill_plan(tp_plan *plan, int threads, int lds, int64_t tiles, int64_t grid, int tile_units)
+void fill_plan(tp_plan *plan, int threads, int lds, int64_t tiles, int64_t grid, int tile_units, int stages = 1)
 {
     if (!plan)
         return;
     memset(plan, 0, sizeof *plan);
-    plan->stages = 1;
+    plan->stages = stages;
     plan->threads = threads;
     plan->lds_bytes = lds;
     plan->ring_bytes = lds;
@@ -331,7 +331,7 @@ int plan_block_quantize(uintptr_t x, int64_t x_stride, int64_t rows, int64_t col
     const int st = check_overlap(outs, ins, false);
     if (st != TP_OK)
         return st;
-    fill_plan(plan, 256, 0, tiles, tiles, kOpBlock);
+    fill_plan(plan, 256, kQuantLdsBytes, tiles, tiles, kOpBlock);
     return TP_OK;
 }
 
@@ -405,7 +405,7 @@ MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k, int out_type)
         int64_t splits = tiles > 0 ? kOpCus / tiles : 1;
         if (splits > blocks / 16)
             splits = blocks / 16;
-        p.waves = 8;
+        p.waves = kSkinnyWaves;
         if (splits > 1 && can_split)
             p.splits = (int)(splits < kMostSplits ? splits : kMostSplits);
         if (m > 16) {
@@ -435,6 +435,19 @@ MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k, int out_type)
                 }
             }
         }
+    }
+    const int64_t groups = op_ceil(m, p.tile_m) * op_ceil(n, p.tile_n) * p.splits;
+    if (p.shape == kMatmulSkinny) {
+        // blocks of a wave: with more than 4 a second slot pays (1 x 16384 x
+        // 8192: 28.3 us against 30.3), with fewer the smaller LDS does (1 x
+        // 8192 x 4096: 9.7 against 10.1); more rows of a fill one slot's time
+        p.stages = p.tile_m == 16 && op_ceil(blocks, p.splits * kSkinnyWaves) > 4 ? 2 : 1;
+        p.lds_bytes = matmul_skinny_lds(p.tile_m, p.stages);
+        p.grid = groups;
+    } else {
+        p.stages = matmul_stages(p.shape);
+        p.lds_bytes = matmul_tile_lds(p.tile_m, p.tile_n, p.stages);
+        p.grid = op_ceil(groups, 8) * 8;     // as many for each XCD
     }
     p.partial_bytes = p.splits > 1 ? p.splits * m * n * 4 : 0;
     return p;
@@ -478,9 +491,9 @@ int plan_block_matmul(uintptr_t a, int64_t a_stride, int a_type, uintptr_t sa, u
         return st;
     const MatmulPlan p = matmul_plan(m, n, k, out_type);
     const int64_t tiles = op_ceil(m, p.tile_m) * op_ceil(n, p.tile_n);
-    if (tiles * p.splits > INT32_MAX - 8)
+    if (p.grid > INT32_MAX)
         return TP_ERR_INVALID_ARG;
-    fill_plan(plan, 64 * p.waves, 0, tiles, tiles * p.splits, p.tile_m);
+    fill_plan(plan, 64 * p.waves, p.lds_bytes, tiles, p.grid, p.tile_m, p.stages);
     return TP_OK;
 }
 

@@ -110,13 +110,37 @@ TP_HD constexpr bool matmul_wide(int out_type) { return out_type != TP_BF16; }
 // How the product is cut; see matmul_plan.
 enum MatmulShape : int32_t { kMatmulSkinny = 0, kMatmul128 = 1, kMatmul128x256 = 2, kMatmul256 = 3, kMatmul64 = 4 };
 
+// Stages of LDS that the operands' blocks pass through.
+TP_HD constexpr int matmul_stages(int shape)
+{
+    // (64 x 64 with a fourth stage: 1 to 3 % slower)
+    return shape == kMatmul64 || shape == kMatmul128x256 ? 3 : 2;
+}
+
+// LDS of a workgroup: the stages, two sets of four blocks' scales, and a place
+// for loads of nothing; of the few-rows kernel, each wave's slots and scales.
+constexpr int kSkinnyWaves = 8;
+TP_HD constexpr int matmul_tile_lds(int tile_m, int tile_n, int stages)
+{
+    return (tile_m + tile_n) * (stages * kOpBlock + 2 * 16) + 1024;
+}
+TP_HD constexpr int matmul_skinny_lds(int tile_m, int slots)
+{
+    return kSkinnyWaves * (tile_m + 16) * (slots * kOpBlock + 2 * 16);
+}
+
 struct MatmulPlan {
     int shape;               // MatmulShape
     int tile_m, tile_n;
     int waves;               // of a workgroup
+    int stages;              // of LDS; slots of each wave of the few-rows kernel
+    int lds_bytes;
     int splits;
+    int64_t grid;            // workgroups
     int64_t partial_bytes;
 };
+
+constexpr int kQuantLdsBytes = 20992;         // of a workgroup of the quantiser
 
 RowPlan norm_plan(int64_t rows, int64_t cols, int type, bool residual);
 RowPlan norm_grad_plan(int64_t rows, int64_t cols, int type, bool more);

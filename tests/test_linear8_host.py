@@ -197,6 +197,38 @@ def test_matmul_tile_shapes():
             assert st == OK and (plan.threads // 64, plan.tile_units) == (narrow if ot == BF16 else wide)
 
 
+def matmul_plan(m, n, k, ot, square=0):
+    plan = tilepipe._CPlan()
+    need = lib().tp_block_matmul_workspace_bytes(m, n, k, ot)
+    st = lib().tp_plan_block_matmul(1 << 44, k, E4M3, 1 << 45, 1 << 46, k, E4M3, 1 << 47, square, m, n, k, 1 << 48, n, ot,
+                                    1 << 49, need, ctypes.byref(plan))
+    assert st == OK
+    return plan, max(1, need // (m * n * 4))
+
+
+def test_matmul_plans_say_what_is_launched():
+    """Stages, LDS and workgroups of each shape: the stages' blocks of 128 bytes,
+    two sets of 16 bytes of scales a row, and 1 KiB; rounded up to the 8 XCDs."""
+    side = {64: (64, 3), 128: (128, 2), 256: (256, 2)}
+    for (m, n, k), _, _ in forms.TILE_SHAPES:
+        for ot in (BF16, FP16, FP32):
+            plan, splits = matmul_plan(m, n, k, ot)
+            wide, stages = (256, 3) if plan.threads == 512 and plan.tile_units == 128 else side[plan.tile_units]
+            assert plan.stages == stages
+            assert plan.lds_bytes == (plan.tile_units + wide) * (stages * 128 + 32) + 1024 <= 160 * 1024
+            assert plan.num_tiles == -(-m // plan.tile_units) * -(-n // wide)
+            assert plan.grid == -(-plan.num_tiles * splits // 8) * 8
+    for (m, n, k), slots in forms.FEW_ROWS:
+        for ot in (BF16, FP16, FP32):
+            plan, splits = matmul_plan(m, n, k, ot)
+            assert (plan.threads, plan.stages, plan.tile_units) == (512, slots, -(-m // 16) * 16)
+            assert plan.lds_bytes == 8 * (plan.tile_units + 16) * (slots * 128 + 32) <= 160 * 1024
+            assert plan.grid == plan.num_tiles * splits == -(-n // 16) * splits
+    plan = tilepipe._CPlan()
+    assert lib().tp_plan_block_quantize(A, 300, 200, 300, BF16, 0, E5M2, B, 304, C, D, 208, E, ctypes.byref(plan)) == OK
+    assert 128 * 128 < plan.lds_bytes <= 40 * 1024 and (plan.threads, plan.grid) == (256, 6)
+
+
 def test_workspace_sizes():
     ws = lib().tp_block_matmul_workspace_bytes
     assert ws(1, 1, 1, BF16) == 0 and ws(0, 5, 5, BF16) == 0
