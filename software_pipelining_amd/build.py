@@ -6,7 +6,8 @@ Translation units compile in parallel into ``_build/`` at the repository root;
 the shared library is written next to this file. The planners (tp_*plan.cpp) are
 plain C++ and are compiled by g++ to keep them free of HIP. The direct binding of
 the 8-bit layer's operators (tp_torch.cpp, against torch's own headers) becomes
-_linear8.so beside the library.
+_linear8.so beside the library; where it cannot be built, the operators are
+called through ctypes.
 """
 from __future__ import annotations
 
@@ -112,8 +113,23 @@ def _link_binding(obj: str) -> None:
     os.replace(tmp, BINDING)
 
 
+def _bind(compiled) -> bool:
+    """Links the binding from its compilation's future. The library needs no torch
+    and linear8.py no binding, so a failure is reported and does not end the
+    build; a binding of an older build goes, since it may not fit the library."""
+    try:
+        _link_binding(compiled.result())
+        return True
+    except Exception as e:  # noqa: BLE001
+        print(f"[build] without the direct binding ({os.path.basename(BINDING)}): {e}", file=sys.stderr)
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        return False
+
+
 def build(jobs: int | None = None, verbose: bool = True, save_temps: bool = False) -> str:
-    """Compile every translation unit and link libtilepipe.so; return its path."""
+    """Compile every translation unit, link libtilepipe.so and the direct binding;
+    return the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     t0 = time.time()
     units = HIP_SOURCES + INSTANCES + CXX_SOURCES
@@ -124,7 +140,7 @@ def build(jobs: int | None = None, verbose: bool = True, save_temps: bool = Fals
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    _link_binding(binding.result())
+    _bind(binding)
     if verbose:
         print(f"[build] {LIB} ({time.time() - t0:.1f}s)", file=sys.stderr)
     return LIB

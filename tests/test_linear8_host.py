@@ -1,6 +1,8 @@
 """Refusals and launch plans of the 8-bit linear layer's operators, without a
 GPU: the C planner with made-up addresses, and the binding's own checks."""
 import ctypes
+import os
+import sys
 
 import pytest
 import torch
@@ -247,6 +249,24 @@ def test_workspace_sizes():
     for cols in (1 << 22, (1 << 23) + 8, (1 << 24) - 1, 1 << 24):
         for dtype in (BF16, FP32):
             assert cols * 4 <= gs(10000, cols, dtype) < 1 << 31
+
+
+def test_build_without_torch_keeps_the_library(monkeypatch, tmp_path, capsys):
+    """The direct binding needs torch's headers; the library does not."""
+    from software_pipelining_amd import build
+    old = tmp_path / "_linear8.so"
+    old.write_bytes(b"of an older build")
+    monkeypatch.setattr(build, "BINDING", str(old))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libtilepipe.so"))
+    monkeypatch.setattr(build, "_compile", lambda unit, save_temps: str(unit))
+    ran = []
+    monkeypatch.setattr(build, "_run", lambda cmd: ran.append(cmd) or open(cmd[cmd.index("-o") + 1], "wb").close())
+    monkeypatch.setitem(sys.modules, "torch", None)
+    monkeypatch.setitem(sys.modules, "torch.utils", None)
+    assert build.build(jobs=2, verbose=False) == str(tmp_path / "libtilepipe.so")
+    assert os.path.exists(build.LIB) and len(ran) == 1
+    assert not old.exists() and "without the direct binding" in capsys.readouterr().err
 
 
 def test_binding_refusals_without_a_gpu():
