@@ -7,6 +7,8 @@ been built; there is no CPU fallback. :mod:`software_pipelining_amd.linear8`
 binds the 8-bit linear layer's operators; it needs torch and is imported when one
 of its names is first used.
 """
+from importlib.util import find_spec
+
 from .tilepipe import (  # noqa: F401
     Align, TilepipeError, Path, Plan, Schedule, chunk_copy, device_check, lds_budget, library_path,
     map_2d, pipelined_map, plan_chunk_copy, plan_map, plan_map_2d, plan_row_shift,
@@ -23,6 +25,9 @@ __all__ = [
 ]
 
 _LINEAR8 = ("BlockQuantized", "RmsNorm", "block_matmul", "block_quantize", "rms_norm", "rms_norm_backward")
+
+if find_spec("torch") is None:      # a star import leaves out what cannot be had
+    __all__ = [n for n in __all__ if n not in _LINEAR8]
 
 
 def __getattr__(name):

@@ -2,6 +2,7 @@
 GPU: the C planner with made-up addresses, and the binding's own checks."""
 import ctypes
 import os
+import subprocess
 import sys
 
 import pytest
@@ -267,6 +268,18 @@ def test_build_without_torch_keeps_the_library(monkeypatch, tmp_path, capsys):
     assert build.build(jobs=2, verbose=False) == str(tmp_path / "libtilepipe.so")
     assert os.path.exists(build.LIB) and len(ran) == 1
     assert not old.exists() and "without the direct binding" in capsys.readouterr().err
+
+
+def test_star_import_without_torch():
+    """The planning calls need no torch, and a star import of them neither."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from software_pipelining_amd import *\n"
+            "assert plan_row_shift(0x1000, 0x2000, 4).threads and 'rms_norm' not in globals()\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(tp.__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+    scope = {}
+    exec("from software_pipelining_amd import *", scope)
+    assert scope["rms_norm"] is tp.rms_norm and scope["RmsNorm"] is tp.RmsNorm
 
 
 def test_binding_refusals_without_a_gpu():
