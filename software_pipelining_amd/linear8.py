@@ -117,6 +117,9 @@ def _eight_bit_empty(rows: int, cols: int, dtype, device):
 
 def _elsewhere(fn, stream, inputs, *args, **kwargs):
     """fn with `stream` current, its inputs marked as used there."""
+    for t in inputs:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}; expected {t.device}")
     with torch.cuda.stream(stream):
         for t in inputs:
             if isinstance(t, torch.Tensor) and t.is_cuda:
