@@ -455,8 +455,9 @@ TP_API int tp_block_quantize(const void *x, int64_t x_stride, int64_t rows, int6
  * them, eight at a time, each eight to within 2^-13 of its largest product for
  * each of the others. workspace holds
  * tp_block_matmul_workspace_bytes(m, n, k, out_type) bytes (often 0, then it
- * may be NULL) and needs no preparation. Row strides are at most 2^22 bytes, k
- * at most 2^22.
+ * may be NULL) and needs no preparation. Row strides of a and b are at most 2^22
+ * bytes and k at most 2^22; min(m, 256) rows of out span at most 2^30 bytes (one
+ * row may have any length).
  */
 TP_API int tp_block_matmul(const void *a, int64_t a_stride, int a_type, const float *a_scale,
                            const void *b, int64_t b_stride, int b_type, const float *b_scale,

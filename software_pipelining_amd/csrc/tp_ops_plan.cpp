@@ -300,6 +300,7 @@ int plan_rms_norm_backward(uintptr_t dy, int64_t dy_stride, uintptr_t x, int64_t
 
 // Rows of a tile are addressed with 32-bit offsets: 256 of them.
 constexpr int64_t kTileMaxPitch = int64_t(1) << 22;
+constexpr int64_t kTileMaxSpan = kTileMaxPitch * 256;
 
 int plan_block_quantize(uintptr_t x, int64_t x_stride, int64_t rows, int64_t cols, int type,
                         int square, int out_type, uintptr_t q, int64_t q_stride, uintptr_t scale,
@@ -472,7 +473,8 @@ int plan_block_matmul(uintptr_t a, int64_t a_stride, int a_type, uintptr_t sa, u
         return TP_ERR_INVALID_ARG;
     const int ob = type_bytes(out_type);
     if (!valid_stride(a_stride, k) || a_stride > kTileMaxPitch || !valid_stride(b_stride, k) ||
-        b_stride > kTileMaxPitch || !valid_stride(out_stride, n) || out_stride * ob > kTileMaxPitch)
+        b_stride > kTileMaxPitch || !valid_stride(out_stride, n) ||
+        (m > 1 && out_stride * ob > kTileMaxSpan / (m < 256 ? m : 256)))
         return TP_ERR_INVALID_ARG;
     fill_plan(plan, 0, 0, 0, 0, 0);
     if (m == 0 || n == 0)
@@ -491,7 +493,7 @@ int plan_block_matmul(uintptr_t a, int64_t a_stride, int a_type, uintptr_t sa, u
         return st;
     const MatmulPlan p = matmul_plan(m, n, k, out_type);
     const int64_t tiles = op_ceil(m, p.tile_m) * op_ceil(n, p.tile_n);
-    if (p.grid > INT32_MAX)
+    if (p.grid * 64 * p.waves > UINT32_MAX)     // lanes of a launch
         return TP_ERR_INVALID_ARG;
     fill_plan(plan, 64 * p.waves, p.lds_bytes, tiles, p.grid, p.tile_m, p.stages);
     return TP_OK;

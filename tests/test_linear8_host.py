@@ -176,6 +176,13 @@ def matmul(a=A, a_s=272, at=E4M3, sa=B, b=C, bs=272, bt=E4M3, sb=D, square=1, m=
     ({"out": 0}, INVALID),
     ({"k": (1 << 22) + 1, "a_s": 1 << 23, "bs": 1 << 23}, INVALID),
     ({"bs": (1 << 22) + 1}, INVALID),
+    ({"m": 1, "n": 5_000_000, "k": 64, "os_": 5_000_000, "ot": FP32, "out": E + (1 << 40)}, OK),       # one long row
+    ({"m": 3, "n": 5_000_000, "k": 64, "os_": 5_000_000, "ot": FP32, "out": E + (1 << 40)}, OK),
+    ({"m": 100, "os_": 5_000_000, "out": E + (1 << 40)}, OK),
+    ({"m": 64, "os_": 1 << 22, "ot": FP32, "out": E + (1 << 40)}, OK),                             # 2^30 bytes of a tile
+    ({"m": 65, "os_": 1 << 22, "ot": FP32, "out": E + (1 << 40)}, INVALID),
+    ({"m": 300, "os_": 1 << 20, "ot": FP32, "out": E + (1 << 40)}, OK),
+    ({"m": 300, "os_": (1 << 20) + 1, "ot": FP32, "out": E + (1 << 40)}, INVALID),
     ({"sa": B + 2}, MISALIGNED),
     ({"out": E + 1}, MISALIGNED),
     ({"out": A}, OVERLAP),
