@@ -26,11 +26,80 @@ namespace dev {
 struct QuantLds {
     uint32_t col_most[4][kOpBlock];
     uint32_t row_most[kOpBlock];
-    float2 row_scale[kOpBlock];      // BlockQuotient's of each block
+    float2 row_scale[kOpBlock];      // Quotients' of each block
     float2 col_scale[kOpBlock];
     alignas(16) uint8_t turned[kOpBlock * kOpBlock];
 };
 static_assert(sizeof(QuantLds) == kQuantLdsBytes, "the planner's");
+
+// Four numbers of a block over its scale, in 8 bits, and what a block's lanes need
+// for that. `unsure` takes bits where that may be one 8-bit number off: then
+// `settle` makes it the right one, given the bits of the block's largest magnitude.
+template <class T, class F>
+struct Quotients {
+    using Q = BlockQuotient<T, F>;
+    __device__ static __forceinline__ float2 make(const BlockScale &b) { return Q::make(b); }
+    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t &)
+    {
+        return pack4<F>(Q::of(Q::ready(x[0]), b), Q::of(Q::ready(x[1]), b),
+                        Q::of(Q::ready(x[2]), b), Q::of(Q::ready(x[3]), b));
+    }
+    __device__ static __forceinline__ void settle(const float (&)[4], float2, uint32_t, uint32_t &) {}
+};
+
+// Numbers of 32 bits can be tensors of 16-bit ones made wider, or whole numbers,
+// which often lie half way between two 8-bit numbers, and their remainder takes
+// more than an fma. So x times MOST / m is taken with that factor 2^-22 too small
+// and too large, more than its own and the product's rounding: where both round
+// to the same 8-bit number, that is the quotient's. Where not (five numbers of a
+// million), x MOST is compared with m times the middle of the two, both of which
+// 64 bits hold exactly. (5000 x 4104 by rows and columns: 35.1 us, by one rounded
+// factor 33.8; in squares, whose turned numbers are the straight ones, 30.3 and 30.6.)
+template <class F>
+struct Quotients<Fp32, F> {
+    __device__ static __forceinline__ float2 make(const BlockScale &b)
+    {
+        return make_float2(b.factor * (1.0f - 0x1p-22f), b.factor * (1.0f + 0x1p-22f));
+    }
+    __device__ static __forceinline__ uint32_t by(const float (&x)[4], float factor)
+    {
+        return pack4<F>(x[0] * factor, x[1] * factor, x[2] * factor, x[3] * factor);
+    }
+    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t &unsure)
+    {
+        const uint32_t q = by(x, b.x);
+        unsure |= q ^ by(x, b.y);
+        return q;
+    }
+    __device__ static __forceinline__ void settle(const float (&x)[4], float2 b, uint32_t most, uint32_t &q)
+    {
+        const uint32_t r = by(x, b.y);
+        if (q == r)
+            return;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t low = q >> (8 * i) & 0xFFu, high = r >> (8 * i) & 0xFFu;
+            const float v = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
+            const float middle = 0.5f * (F::wide(low & 0x7Fu) + F::wide(high & 0x7Fu));
+            const double is = (double)fabsf(v) * (double)F::most;
+            const double half = (double)middle * (double)__uint_as_float(max(most, kLeastMost));
+            if (is > half || (is == half && (high & 1u) == 0u))
+                q ^= (low ^ high) << (8 * i);
+        }
+    }
+};
+
+// Columns of 4 x 4 bytes from its rows.
+__device__ __forceinline__ void turn4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_t &c0,
+                                      uint32_t &c1, uint32_t &c2, uint32_t &c3)
+{
+    const uint32_t a = __builtin_amdgcn_perm(r1, r0, 0x05010400u), b = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
+    const uint32_t c = __builtin_amdgcn_perm(r1, r0, 0x07030602u), d = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
+    c0 = __builtin_amdgcn_perm(b, a, 0x05040100u);
+    c1 = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    c2 = __builtin_amdgcn_perm(d, c, 0x05040100u);
+    c3 = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
 
 // The elements of a row of fewer than eight.
 template <class T>
@@ -51,7 +120,7 @@ __device__ __forceinline__ RawUnit<T> get_narrow_row(const BufferRes &r, uint32_
 template <class T, class F, bool Square, bool Straight, bool Turned>
 __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_kernel(QuantParams p)
 {
-    using Q = BlockQuotient<T, F>;
+    using Q = Quotients<T, F>;
     __shared__ QuantLds lds;
     const uint32_t tid = threadIdx.x, u = tid % kLanesPerBlock, patch = tid / kLanesPerBlock;
     const uint32_t wave = uniform(tid >> 6);
@@ -121,7 +190,7 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
     }
 
     // ---- the maxima
-    uint32_t row_most[8], col_most[8];
+    uint32_t row_most[8], col_most[8], square_most = 0;
     {
         Magnitudes<T> down_most;
 #pragma unroll
@@ -153,11 +222,10 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
         lds.row_most[wave] = m;
         lds_sync();
         m = max(max(lds.row_most[0], lds.row_most[1]), max(lds.row_most[2], lds.row_most[3]));
+        square_most = m;
         const BlockScale b = block_scale<F>(m);
-        if (tid < kOpBlock) {
-            lds.row_scale[tid] = BlockQuotient<T, F>::make(b);
-            lds.col_scale[tid] = BlockQuotient<T, F>::make(b);
-        }
+        if (tid < kOpBlock)
+            lds.row_scale[tid] = Q::make(b);
         if (wave == 0) {
             const int64_t rows_of_scale = down;
             if constexpr (Straight)
@@ -193,7 +261,7 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
         if (wave < 2) {
             if constexpr (Straight) {
                 const BlockScale b = block_scale<F>(lds.row_most[tid]);
-                lds.row_scale[tid] = BlockQuotient<T, F>::make(b);
+                lds.row_scale[tid] = Q::make(b);
                 const BufferRes rs = make_buffer_res(p.scale + row0 * across + block_col,
                                                      ((high - 1) * across + 1) * 4);
                 put_b32(rs, tid < high ? tid * across * 4 : kOutside, __float_as_uint(b.scale));
@@ -204,7 +272,8 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
                 const uint32_t m = max(max(lds.col_most[0][c], lds.col_most[1][c]),
                                        max(lds.col_most[2][c], lds.col_most[3][c]));
                 const BlockScale b = block_scale<F>(m);
-                lds.col_scale[c] = BlockQuotient<T, F>::make(b);
+                lds.col_scale[c] = Q::make(b);
+                lds.col_most[0][c] = m;      // (which this lane alone has read)
                 const BufferRes rs = make_buffer_res(p.scale_t + col0 * down + block_row,
                                                      ((wide - 1) * down + 1) * 4);
                 put_b32(rs, c < wide ? c * down * 4 : kOutside, __float_as_uint(b.scale));
@@ -216,49 +285,81 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
     // ---- the outputs
     // (the numbers are unpacked again for each: kept unpacked they would take
     // the registers of a fourth workgroup on the CU)
+    uint32_t q[8][2];
+    if constexpr (Straight || Square) {
+        uint32_t unsure = 0;
+        const auto row = [&](int i, auto &&each) TP_INLINE {
+            float v[kUnit];
+            unit_wide<T>(raw[i], v);
+            const float2 b = lds.row_scale[patch * 8 + i];
+            each({v[0], v[1], v[2], v[3]}, b, q[i][0]);
+            each({v[4], v[5], v[6], v[7]}, b, q[i][1]);
+        };
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            row(i, [&](const float (&x)[4], float2 b, uint32_t &to) TP_INLINE { to = Q::of(x, b, unsure); });
+        if (unsure != 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                row(i, [&](const float (&x)[4], float2 b, uint32_t &to) TP_INLINE {
+                    Q::settle(x, b, Square ? square_most : lds.row_most[patch * 8 + i], to);
+                });
+        }
+    }
     if constexpr (Straight) {
         const uint32_t qp = (uint32_t)p.q_stride;
         const BufferRes rq = make_buffer_res(p.q + row0 * p.q_stride + col0, (high - 1) * qp + wide);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 b = lds.row_scale[patch * 8 + i];
-            float v[kUnit];
-            unit_wide<T>(raw[i], v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = Q::of(Q::ready(v[j]), b);
-            const u32x2 q = {pack4<F>(v[0], v[1], v[2], v[3]), pack4<F>(v[4], v[5], v[6], v[7])};
             const bool inside = patch * 8 + i < high;
-            put_b64(rq, have == kUnit && inside ? (patch * 8 + i) * qp + c0 : kOutside, q);
+            put_b64(rq, have == kUnit && inside ? (patch * 8 + i) * qp + c0 : kOutside, u32x2{q[i][0], q[i][1]});
             if (wide % kUnit != 0)
                 put_first_bytes(rq, (patch * 8 + i) * qp + c0, have != 0 && have != kUnit && inside,
-                                wide % kUnit, u32x4{q.x, q.y, 0, 0});
+                                wide % kUnit, u32x4{q[i][0], q[i][1], 0, 0});
         }
     }
-    if constexpr (T::bytes == 2) {
+    if constexpr (T::bytes == 2 && !Square) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             asm volatile("" : "+v"(raw[i].c[0]));
     }
     if constexpr (Turned) {
         // column 8u + j as 8 bytes at piece `patch` of its 16
-        u32x2 q[kUnit];
+        uint32_t t[kUnit][2];
+        if constexpr (Square) {       // the same numbers
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float v[4][kUnit];
+            for (int j = 0; j < 8; j += 4)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                unit_wide<T>(raw[half * 4 + i], v[i]);
+                for (int half = 0; half < 2; ++half)
+                    turn4(q[4 * half][j / 4], q[4 * half + 1][j / 4], q[4 * half + 2][j / 4], q[4 * half + 3][j / 4],
+                          t[j][half], t[j + 1][half], t[j + 2][half], t[j + 3][half]);
+        } else {
+            uint32_t unsure = 0;
+            const auto columns = [&](int half, auto &&each) TP_INLINE {
+                float v[4][kUnit];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 b = lds.col_scale[c0 + j];
-                q[j][half] = pack4<F>(Q::of(Q::ready(v[0][j]), b), Q::of(Q::ready(v[1][j]), b),
-                                      Q::of(Q::ready(v[2][j]), b), Q::of(Q::ready(v[3][j]), b));
+                for (int i = 0; i < 4; ++i)
+                    unit_wide<T>(raw[half * 4 + i], v[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    each({v[0][j], v[1][j], v[2][j], v[3][j]}, j, t[j][half]);
+            };
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                columns(half, [&](const float (&x)[4], int j, uint32_t &to) TP_INLINE {
+                    to = Q::of(x, lds.col_scale[c0 + j], unsure);
+                });
+            if (unsure != 0) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    columns(half, [&](const float (&x)[4], int j, uint32_t &to) TP_INLINE {
+                        Q::settle(x, lds.col_scale[c0 + j], lds.col_most[0][c0 + j], to);
+                    });
             }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<u32x2 *>(lds.turned + (c0 + j) * kOpBlock + (patch ^ u) * 8) = q[j];
+            *reinterpret_cast<u32x2 *>(lds.turned + (c0 + j) * kOpBlock + (patch ^ u) * 8) = u32x2{t[j][0], t[j][1]};
         lds_sync();
         const uint32_t tp_ = (uint32_t)p.qt_stride;
         const BufferRes rq = make_buffer_res(p.qt + col0 * p.qt_stride + row0, (wide - 1) * tp_ + high);

@@ -428,6 +428,11 @@ struct E4m3 {
     {
         return __builtin_amdgcn_cvt_pk_fp8_f32(a, b, old, Hi);
     }
+    // the number that the lowest byte stands for
+    __device__ static __forceinline__ float wide(uint32_t byte)
+    {
+        return __builtin_amdgcn_cvt_f32_fp8((int)byte, 0);
+    }
 };
 
 struct E5m2 {
@@ -436,6 +441,10 @@ struct E5m2 {
     __device__ static __forceinline__ uint32_t pack2(float a, float b, uint32_t old)
     {
         return __builtin_amdgcn_cvt_pk_bf8_f32(a, b, old, Hi);
+    }
+    __device__ static __forceinline__ float wide(uint32_t byte)
+    {
+        return __builtin_amdgcn_cvt_f32_bf8((int)byte, 0);
     }
 };
 
@@ -469,7 +478,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t most_bits)
 // x * (MOST / m) would then decide instead of the tie rule. So for those types
 // the quotient is corrected by its remainder: MOST is 7/8 of a power of two, so
 // x * 7/8 and the divisor, m over that power, are exact, and so is the fma's
-// remainder. (For numbers of 32 bits a tie is as rare as any other value.)
+// remainder. (A product of two fp32 numbers, the norm's, is rounded itself, and a
+// tie there is as rare as any other value.)
 template <class T, class F>
 struct BlockQuotient {
     static constexpr bool exact = T::bytes == 2;
