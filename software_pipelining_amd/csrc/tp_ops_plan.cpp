@@ -89,7 +89,10 @@ int64_t even_grid(int64_t rows, int64_t most)
 // few of them stream best: the rows in flight then lie close together (8192 x
 // 8192 bf16 with a residual: 86 us with 4 waves a CU, 90 with 8, 95 with 12;
 // the gradient of 8192 x 4096: 52, 56, 61). With fewer rows it is their number
-// in flight that counts (777 x 5003: 11.5 us with 4, 7.5 with 16).
+// in flight that counts (777 x 5003: 11.5 us with 4, 7.5 with 16). The rule counts
+// rows, not bytes, and so serves narrow ones badly: 8192 x 128 bf16 with a
+// residual takes 8.8 us with 4 waves a CU, 8191 x 128 6.0 with 16; 524288 x 128
+// (474 MB) 360.
 constexpr int kRowWavesPerCu = 4;
 constexpr int kFewRowsWavesPerCu = 16;
 // The gradient writes and adds a row of partial sums for each workgroup, and
@@ -200,6 +203,8 @@ RowPlan norm_grad_plan(int64_t rows, int64_t cols, int type, bool more)
         p.waves = bytes == 4 ? 2 : 4;
         p.lds_bytes = kRowRedBytes + p.waves * (row_wave_lds(4, kRowUnits, bytes) + kRowCutBytes);
         // all partial sums of dw lie below the offset that stands for no place
+        // (dx is made by as few workgroups, which leaves most CUs idle: 4096 x
+        // 18432 bf16 with a second gradient 850 us, its bytes 90)
         const int64_t most = (int64_t(1) << 30) / (partial_pitch(cols) * 4);
         p.grid = even_grid(rows, most < kOpCus / 4 ? most : kOpCus / 4);
     } else if (!more) {
@@ -390,7 +395,7 @@ double tile_cost(const ShapeCost &c, int64_t m, int64_t n, int64_t blocks, int s
 // a once for every 16 columns; where that is several rows for one of b and
 // takes several rounds of workgroups, its cost is compared with the tiles' (64
 // x 16384 x 4096 into bf16: 26.3 us, 21.3 by tiles; 32 x 64000 x 2048: 45.6 and
-// 32.2; 64 x 4096 x 4096, one round: 8.5 and 13.2).
+// 29.9; 64 x 4096 x 4096, one round: 8.5 and 13.2).
 MatmulPlan matmul_plan(int64_t m, int64_t n, int64_t k, int out_type)
 {
     MatmulPlan p{};

@@ -256,8 +256,11 @@ def block_quantize(x, out_format: str = "e4m3", square: bool = False, straight: 
 def block_matmul(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, stream=None):
     """(m, n) = A B^T of 8-bit matrices a (m, k) and b (n, k), each e4m3 or
     e5m2, with a_scale (m, ceil(k / 128)) and b_scale (n, ceil(k / 128)) or, for
-    a weight in squares, (ceil(n / 128), ceil(k / 128)). Sums are float32,
-    rounded once to out_dtype (bfloat16, float16 or float32)."""
+    a weight in squares, (ceil(n / 128), ceil(k / 128)). Blocks are added in
+    float32 and rounded once to out_dtype (bfloat16, float16 or float32). So are
+    the 128 products of a block for float16 and float32; for bfloat16 the 8-bit
+    matrix instructions add them, each eight to within 2^-13 of its largest
+    product for each of the others."""
     if stream is not None:
         return _elsewhere(block_matmul, stream, (a, a_scale, b, b_scale), a, a_scale, b, b_scale, out_dtype)
     if _direct is not None:
