@@ -33,13 +33,14 @@ struct QuantLds {
 static_assert(sizeof(QuantLds) == kQuantLdsBytes, "the planner's");
 
 // Four numbers of a block over its scale, in 8 bits, and what a block's lanes need
-// for that. `unsure` takes bits where that may be one 8-bit number off: then
-// `settle` makes it the right one, given the bits of the block's largest magnitude.
+// for that. `unsure` takes `bit` where one of them may be the 8-bit number below
+// the right one: then `settle` makes it right, given the bits of the block's
+// largest magnitude.
 template <class T, class F>
 struct Quotients {
     using Q = BlockQuotient<T, F>;
     __device__ static __forceinline__ float2 make(const BlockScale &b) { return Q::make(b); }
-    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t &)
+    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t, uint32_t &)
     {
         return pack4<F>(Q::of(Q::ready(x[0]), b), Q::of(Q::ready(x[1]), b),
                         Q::of(Q::ready(x[2]), b), Q::of(Q::ready(x[3]), b));
@@ -54,7 +55,9 @@ struct Quotients {
 // to the same 8-bit number, that is the quotient's. Where not (five numbers of a
 // million), x MOST is compared with m times the middle of the two, both of which
 // 64 bits hold exactly. (5000 x 4104 by rows and columns: 35.1 us, by one rounded
-// factor 33.8; in squares, whose turned numbers are the straight ones, 30.3 and 30.6.)
+// factor 33.8; in squares, whose turned numbers are the straight ones, 30.3 and 30.6.
+// Of bf16 values made wider three of ten thousand lie on ties: again and again on
+// one tensor 38.0 and 29.1 us, 29.3 and 25.2 of any numbers.)
 template <class F>
 struct Quotients<Fp32, F> {
     __device__ static __forceinline__ float2 make(const BlockScale &b)
@@ -65,26 +68,26 @@ struct Quotients<Fp32, F> {
     {
         return pack4<F>(x[0] * factor, x[1] * factor, x[2] * factor, x[3] * factor);
     }
-    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t &unsure)
+    __device__ static __forceinline__ uint32_t of(const float (&x)[4], float2 b, uint32_t bit, uint32_t &unsure)
     {
         const uint32_t q = by(x, b.x);
-        unsure |= q ^ by(x, b.y);
+        unsure |= q != by(x, b.y) ? bit : 0u;
         return q;
     }
     __device__ static __forceinline__ void settle(const float (&x)[4], float2 b, uint32_t most, uint32_t &q)
     {
         const uint32_t r = by(x, b.y);
-        if (q == r)
-            return;
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t low = q >> (8 * i) & 0xFFu, high = r >> (8 * i) & 0xFFu;
-            const float v = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
+        for (uint32_t left = q ^ r; left != 0;) {
+            const uint32_t at = (uint32_t)__builtin_ctz(left) & 24u;
+            left &= ~(0xFFu << at);
+            const uint32_t low = q >> at & 0xFFu, high = r >> at & 0xFFu;
+            const float v = at < 16 ? (at == 0 ? x[0] : x[1]) : at == 16 ? x[2] : x[3];
             const float middle = 0.5f * (F::wide(low & 0x7Fu) + F::wide(high & 0x7Fu));
             const double is = (double)fabsf(v) * (double)F::most;
             const double half = (double)middle * (double)__uint_as_float(max(most, kLeastMost));
             if (is > half || (is == half && (high & 1u) == 0u))
-                q ^= (low ^ high) << (8 * i);
+                q ^= (low ^ high) << at;
         }
     }
 };
@@ -291,18 +294,22 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
         const auto row = [&](int i, auto &&each) TP_INLINE {
             float v[kUnit];
             unit_wide<T>(raw[i], v);
-            const float2 b = lds.row_scale[patch * 8 + i];
-            each({v[0], v[1], v[2], v[3]}, b, q[i][0]);
-            each({v[4], v[5], v[6], v[7]}, b, q[i][1]);
+            each({v[0], v[1], v[2], v[3]}, 1u << (2 * i), q[i][0]);
+            each({v[4], v[5], v[6], v[7]}, 2u << (2 * i), q[i][1]);
         };
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            row(i, [&](const float (&x)[4], float2 b, uint32_t &to) TP_INLINE { to = Q::of(x, b, unsure); });
+        for (int i = 0; i < 8; ++i) {
+            const float2 b = lds.row_scale[patch * 8 + i];
+            row(i, [&](const float (&x)[4], uint32_t bit, uint32_t &to) TP_INLINE {
+                to = Q::of(x, b, bit, unsure);
+            });
+        }
         if (unsure != 0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                row(i, [&](const float (&x)[4], float2 b, uint32_t &to) TP_INLINE {
-                    Q::settle(x, b, Square ? square_most : lds.row_most[patch * 8 + i], to);
+                row(i, [&](const float (&x)[4], uint32_t bit, uint32_t &to) TP_INLINE {
+                    if (unsure & bit)
+                        Q::settle(x, lds.row_scale[patch * 8 + i], Square ? square_most : lds.row_most[patch * 8 + i], to);
                 });
         }
     }
@@ -342,18 +349,19 @@ __global__ void __launch_bounds__(256, T::bytes == 2 ? 4 : 3) block_quantize_ker
                     unit_wide<T>(raw[half * 4 + i], v[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    each({v[0][j], v[1][j], v[2][j], v[3][j]}, j, t[j][half]);
+                    each({v[0][j], v[1][j], v[2][j], v[3][j]}, j, 1u << (2 * j + half), t[j][half]);
             };
 #pragma unroll
             for (int half = 0; half < 2; ++half)
-                columns(half, [&](const float (&x)[4], int j, uint32_t &to) TP_INLINE {
-                    to = Q::of(x, lds.col_scale[c0 + j], unsure);
+                columns(half, [&](const float (&x)[4], int j, uint32_t bit, uint32_t &to) TP_INLINE {
+                    to = Q::of(x, lds.col_scale[c0 + j], bit, unsure);
                 });
             if (unsure != 0) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
-                    columns(half, [&](const float (&x)[4], int j, uint32_t &to) TP_INLINE {
-                        Q::settle(x, lds.col_scale[c0 + j], lds.col_most[0][c0 + j], to);
+                    columns(half, [&](const float (&x)[4], int j, uint32_t bit, uint32_t &to) TP_INLINE {
+                        if (unsure & bit)
+                            Q::settle(x, lds.col_scale[c0 + j], lds.col_most[0][c0 + j], to);
                     });
             }
         }
